@@ -10,37 +10,47 @@ namespace mx {
 // ---- few output tiles: the eight waves of a block split the contraction ----
 // The kernel of gemm.hip runs a tile's contraction as one chain of k-steps, about 0.4 us each;
 // with fewer tiles than compute units the chain is all there is (32 x 4096 outputs over 4096:
-// 25 us on 32 units, where the operands take 3 us to read). Here a block takes a tile of TM x
+// 20 us on 32 units, where the operands take 3 us to read; 8 us here). Here a block takes a tile of TM x
 // TN (64 or 32) and each wave every eighth 64-byte chunk of the contraction, which it brings
 // into LDS of its own, one chunk ahead; the partial tiles meet in LDS, and every thread then
 // finishes eight consecutive columns of one row. Nothing waits at a barrier inside the
 // contraction. EP_SWIGLU: TN = 64, a band of 32 gate rows and one of 32 up rows.
-template <int TM, int TN>
+// The chunk ahead stays in flight behind a counted wait, so every chunk issues the same LOADS
+// instructions whatever lies inside the operands: codes and scales alike come in by LDS loads
+// whose descriptors end with the operand, and what lies past that is zeros. (Scales loaded into
+// registers under a branch on their band leave the count short where the band is absent.)
+template <int TM, int TN, int EL>
 struct SmallTile {
   static constexpr int PITCH = TN + 4;           // floats per row of a partial tile
-  static constexpr int CHUNK = (TM + TN) * 64;   // one chunk of both operands
+  static constexpr int CODES = (TM + TN) * 64;   // one chunk of both operands
+  static constexpr int BANDS = EL == EL_MXFP8 ? (TM + TN) / 32 : 0;  // 256 bytes of scales each
+  static constexpr int CHUNK = CODES + BANDS * 256;
+  static constexpr int LOADS = CODES / 1024 + BANDS;  // of a chunk, per wave
   static constexpr int PARTS = 8 * TM * PITCH * 4, RING = 8 * 2 * CHUNK;
   static constexpr int LDS = PARTS > RING ? PARTS : RING;
 };
 
 // ROWS operand rows, 64-byte chunk c of each, into LDS: piece q of row r at r * 64 + (q ^ ((r >>
 // 2) & 3)) * 16, so that sixteen rows at one piece hit different banks. Rows past the
-// descriptor's end and pieces past the contraction come in as zeros.
+// descriptor's end and pieces past the contraction come in as zeros. The offset is opaque to the
+// compiler, which otherwise makes two loads, one for each side of the choice.
 template <int ROWS>
 __device__ __forceinline__ void load_pieces(__amdgpu_buffer_rsrc_t rsrc, unsigned pitch, int c, uint8_t* dst, int l) {
 #pragma unroll
   for (int i = 0; i < ROWS / 16; ++i) {
     const int r = 16 * i + (l >> 2);
     const unsigned k = (unsigned)c * 64 + ((l & 3) ^ ((r >> 2) & 3)) * 16;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr_t)(dst + i * 1024), 16,
-                                             k < pitch ? (unsigned)r * pitch + k : 0x80000000u, 0, 0, 0);
+    unsigned off = k < pitch ? (unsigned)r * pitch + k : 0x80000000u;
+    asm("" : "+v"(off));
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr_t)(dst + i * 1024), 16, off, 0, 0, 0);
   }
 }
 
 template <int TM, int TN, int EL, int OUT_BF16, int EP>
 __global__ __launch_bounds__(512, 2) void k_epi_small(EpiArgs p) {
   constexpr bool GLU = EP == EP_SWIGLU, SCALED = EL == EL_MXFP8;
-  constexpr int IM = TM / 32, IN = TN / 32, PITCH = SmallTile<TM, TN>::PITCH, CHUNK = SmallTile<TM, TN>::CHUNK;
+  using S = SmallTile<TM, TN, EL>;
+  constexpr int IM = TM / 32, IN = TN / 32, PITCH = S::PITCH, CHUNK = S::CHUNK;
   static_assert(!GLU || TN == 64, "a gate band and an up band");
   extern __shared__ __attribute__((aligned(16))) float parts[];  // [8][TM][PITCH]
   const int tid = threadIdx.x, l = tid & 63, h = l >> 5;
@@ -73,8 +83,18 @@ __global__ __launch_bounds__(512, 2) void k_epi_small(EpiArgs p) {
       __builtin_amdgcn_make_buffer_rsrc((void*)(p.b + b_first * p.ldb), (short)0, (int)(b_rows * p.ldb), 0x00020000);
   const __amdgpu_buffer_rsrc_t ru = __builtin_amdgcn_make_buffer_rsrc(
       (void*)(p.b + (b_first + (GLU ? p.N / 2 : 0)) * p.ldb), (short)0, (int)(b_rows * p.ldb), 0x00020000);
+  // the scales of the tile's bands, A's, then B's (EP_SWIGLU: the gate band and, b_step further, the up band)
+  const int64_t a_band = row0 / 32, b_band = b_first / 32, b_step = GLU ? p.N / 64 : 1;
+  const int64_t a_left = (p.a_rows + 31) / 32 - a_band, b_left = (p.b_rows + 31) / 32 - b_band;
+  const int64_t a_bands = a_left < IM ? a_left : IM, b_bands = GLU ? b_step + 1 : (b_left < IN ? b_left : IN);
+  const __amdgpu_buffer_rsrc_t rsa = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)(p.a_s + a_band * p.a_ktiles * 256), (short)0, (int)(SCALED ? a_bands * p.a_ktiles * 256 : 0), 0x00020000);
+  const __amdgpu_buffer_rsrc_t rsb = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)(p.b_s + b_band * p.b_ktiles * 256), (short)0, (int)(SCALED ? b_bands * p.b_ktiles * 256 : 0), 0x00020000);
   const int chunks = (int)((p.lda + 63) / 64);
   uint8_t* ring = (uint8_t*)parts + wave * 2 * CHUNK;
+  // chunk c of both operands, with its 256-wide scale windows (lane l: row l % 32, block parity
+  // l / 32; the chunk's byte is c % 4): S::LOADS instructions
   auto load = [&](int c, int buf) {
     uint8_t* dst = ring + buf * CHUNK;
     load_pieces<TM>(ra, pitch, c, dst, l);
@@ -84,44 +104,25 @@ __global__ __launch_bounds__(512, 2) void k_epi_small(EpiArgs p) {
     } else {
       load_pieces<TN>(rb, pitch, c, dst + TM * 64, l);
     }
-  };
-  // scale dwords of a chunk's 256-wide window (lane l: row l % 32, block parity l / 32), the
-  // chunk's byte moved down; bands past the operand are all zero rows
-  struct Scales {
-    unsigned a[IM], b[IN];
-  };
-  const int64_t a_bands = (p.a_rows + 31) / 32, b_bands = (p.b_rows + 31) / 32;
-  auto scales = [&](int c) {
-    Scales s;
     if constexpr (SCALED) {
 #pragma unroll
-      for (int i = 0; i < IM; ++i) {
-        const int64_t band = row0 / 32 + i;
-        s.a[i] = band < a_bands ? *(const unsigned*)(p.a_s + (band * p.a_ktiles + (c >> 2)) * 256 + 4 * l) >> ((c & 3) * 8) : 0u;
-      }
-#pragma unroll
-      for (int j = 0; j < IN; ++j) {
-        const int64_t band = (b_first + (GLU ? j * (p.N / 2) : j * 32)) / 32;
-        s.b[j] = band < b_bands ? *(const unsigned*)(p.b_s + (band * p.b_ktiles + (c >> 2)) * 256 + 4 * l) >> ((c & 3) * 8) : 0u;
+      for (int t = 0; t < IM + IN; ++t) {
+        const unsigned band = t < IM ? (unsigned)t * (unsigned)p.a_ktiles : (unsigned)((t - IM) * b_step * p.b_ktiles);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(t < IM ? rsa : rsb, (lds_ptr_t)(dst + S::CODES + t * 256), 4,
+                                                 (band + (c >> 2)) * 256 + 4 * l, 0, 0, 0);
       }
     }
-    return s;
   };
   v16f acc[IM][IN];
 #pragma unroll
   for (int i = 0; i < IM; ++i)
 #pragma unroll
     for (int j = 0; j < IN; ++j) acc[i][j] = (v16f){};
-  Scales cur{}, nxt{};
-  if (wave < chunks) {
-    cur = scales(wave);
-    load(wave, 0);
-  }
+  if (wave < chunks) load(wave, 0);
   for (int c = wave, buf = 0; c < chunks; c += 8, buf ^= 1) {
     if (c + 8 < chunks) {
-      nxt = scales(c + 8);
       load(c + 8, buf ^ 1);
-      MX_WAIT_VMCNT((TM + TN) / 16 + (SCALED ? IM + IN : 0));  // all of chunk c, with its scales
+      MX_WAIT_VMCNT(S::LOADS);  // all of chunk c
     } else {
       MX_WAIT_VMCNT(0);
     }
@@ -134,6 +135,12 @@ __global__ __launch_bounds__(512, 2) void k_epi_small(EpiArgs p) {
         const int r = 32 * t + (l & 31);
         f[t][q] = *(const u32x4*)(ring + buf * CHUNK + r * 64 + (((h + 2 * q) ^ ((r >> 2) & 3)) << 4));
       }
+    int sc[IM + IN] = {};
+    if constexpr (SCALED) {
+#pragma unroll
+      for (int t = 0; t < IM + IN; ++t)
+        sc[t] = (int)(*(const unsigned*)(ring + buf * CHUNK + S::CODES + t * 256 + 4 * l) >> ((c & 3) * 8));
+    }
 #pragma unroll
     for (int i = 0; i < IM; ++i)
 #pragma unroll
@@ -142,14 +149,14 @@ __global__ __launch_bounds__(512, 2) void k_epi_small(EpiArgs p) {
         if constexpr (SCALED) {
           const v8i a = (v8i){(int)a0[0], (int)a0[1], (int)a0[2], (int)a0[3], (int)a1[0], (int)a1[1], (int)a1[2], (int)a1[3]};
           const v8i b = (v8i){(int)b0[0], (int)b0[1], (int)b0[2], (int)b0[3], (int)b1[0], (int)b1[1], (int)b1[2], (int)b1[3]};
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, acc[i][j], 0, 0, 0, (int)cur.b[j], 0, (int)cur.a[i]);
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, acc[i][j], 0, 0, 0, sc[IM + j], 0, sc[i]);
         } else {
           acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, b0), __builtin_bit_cast(bf16x8, a0), acc[i][j], 0, 0, 0);
           acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, b1), __builtin_bit_cast(bf16x8, a1), acc[i][j], 0, 0, 0);
         }
       }
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the next load overwrites what was read here
     lds_fence();
-    cur = nxt;
   }
   __syncthreads();  // every wave is done with its ring, which the partial tiles overlie
 #pragma unroll
@@ -227,10 +234,10 @@ __global__ __launch_bounds__(512, 2) void k_epi_small(EpiArgs p) {
 namespace {
 
 // The tiling. Up to a round of 64x64 tiles, k_epi_small: 64x64 tiles, 32x64 up to half a round,
-// 32x32 where contraction rows above 4 KB then still leave units idle (us, the kernel of
-// gemm.hip / 64x64 / 32x64 / 32x32: 32 x 4096 over 4096 MXFP8 24 / 11 / 10 / 11, bf16 37 / 17 / 16
-// / 11; 512 x 512 over 4096 bf16 36 / 22 / 16 / 11; 1024 x 1024 over 4096 MXFP8 26 / 20 / 30 / 24;
-// above: 512 x 4096 over 4096 27 / 41 / 60 / 48). Then few output tiles take quarter-size ones, short contractions and little more than
+// 32x32 where contraction rows above 4 KB then still leave units idle (kernel us, the kernel of
+// gemm.hip / 64x64 / 32x64 / 32x32: 32 x 4096 over 4096 MXFP8 20 / 10 / 8 / 8, bf16 31 / 16 / 16
+// / 11; 512 x 512 over 4096 MXFP8 19 / 10 / 8 / 8, bf16 30 / 20 / 15 / 12; 1024 x 1024 over 4096
+// MXFP8 20 / 14 / 18 / 19; above: 512 x 4096 over 4096 21 / 29 / 35 / 36). Then few output tiles take quarter-size ones, short contractions and little more than
 // half a round of the compute units 128x256 tiles, two blocks per unit, all else 256x256 ones
 // with two waves per SIMD (one wave holding 256 sums is no faster beside a residual, 660 to 667
 // against 655 to 666 for 32768 x 7168 over 2048, and spills without one); two
@@ -241,7 +248,7 @@ namespace {
 // 4096 353 / 302 / 282, and 269 with the quarters.
 template <int TM, int TN, int EL, int OUT, int EP>
 hipError_t launch_epi_small(mx::EpiArgs p, hipStream_t stream) {
-  constexpr int lds = mx::SmallTile<TM, TN>::LDS;
+  constexpr int lds = mx::SmallTile<TM, TN, EL>::LDS;
   static const hipError_t attr = hipFuncSetAttribute((const void*)mx::k_epi_small<TM, TN, EL, OUT, EP>,
                                                      hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (attr != hipSuccess) return attr;

@@ -386,3 +386,52 @@ def test_refusals():
         mx.mx_epilogue_backward(z, z, None, SILU, workspace=None)
     with pytest.raises(ValueError, match="rows"):
         mx.mx_epilogue_backward(z[:3], z, None, SILU)
+
+
+# ---- contractions that go round the chunk ring of the few-tile kernel --------------------
+# Eight waves take 64-byte chunks in turn, so rows above 512 bytes give a wave a second chunk
+# and above 1024 bytes reuse its first buffer. 32x64 tiles, 64x64 ones (129 to 256 tiles of 64x64)
+# and 32x32 ones (rows above 4096 bytes); m and n that end 1 to 32 rows into a 64-wide tile,
+# whose second band of scales is absent; contractions that end inside a chunk.
+RING = [
+    # kind, m, n, k, group sizes, act, bias, residual, pre, out
+    ("mx", 40, 100, 4096, None, SILU, True, True, True, F32),
+    ("mx", 84, 96, 1056, [32, 0, 32], NONE, True, True, False, BF16),
+    ("mx", 33, 192, 4096, None, SWIGLU, True, True, True, BF16),
+    ("mx", 96, 128, 2080, [32, 64], SWIGLU, False, False, True, F32),
+    ("mx", 40, 72, 4128, None, GELU, True, True, True, BF16),
+    ("mx", 65, 33, 4128, None, NONE, False, False, False, F32),
+    ("mx", 96, 64, 4224, [64, 32], RELU, True, True, True, F32),
+    ("mx", 84, 4116, 1056, None, NONE, True, True, True, F32),
+    ("mx", 65, 4097, 544, None, GELU, True, True, True, BF16),
+    ("mx", 20, 8288, 1120, None, SILU, False, False, False, F32),
+    ("mx", 84, 4224, 1056, None, SWIGLU, True, True, True, BF16),
+    ("mx", 96, 2080, 608, [32, 0, 64], SILU, True, False, True, F32),
+    ("bf16", 40, 100, 2048, None, SILU, True, True, True, F32),
+    ("bf16", 90, 192, 1032, [1, 0, 80], SWIGLU, True, True, True, BF16),
+    ("bf16", 40, 72, 2056, None, GELU, True, True, True, F32),
+    ("bf16", 50, 40, 2184, [17, 30], NONE, True, False, True, BF16),
+    ("bf16", 84, 4116, 552, None, RELU, True, True, True, F32),
+    ("bf16", 84, 4224, 600, None, SWIGLU, True, True, True, F32),
+]
+
+
+@pytest.mark.parametrize("case", RING, ids=["-".join(map(str, c[:4])) + f"-act{c[5]}" for c in RING])
+def test_forward_long_contractions(oracle, case):
+    test_forward(oracle, case)
+
+
+@pytest.mark.parametrize("kind,m,n,k,act", [("mx", 84, 4116, 1056, NONE), ("mx", 40, 72, 4128, NONE),
+                                            ("mx", 33, 192, 4096, SWIGLU), ("bf16", 84, 4116, 552, NONE)])
+def test_forward_long_contractions_same_bits(kind, m, n, k, act):
+    """Operands from memory and from the caches: the same bits however long the loads take."""
+    a = torch.randn(m, k, device="cuda:0").bfloat16()
+    b = (torch.randn(n, k, device="cuda:0") * k**-0.5).bfloat16()
+    ops = (a, b) if kind == "bf16" else (*mx.mx_quantize_dim0(a), *mx.mx_quantize_dim0(b))
+    f = mx.mx_grouped_mm_bf16_fwd_epilogue if kind == "bf16" else mx.mx_grouped_mm_fwd_epilogue
+    want = f(*ops, None, m, n, k, act=act, out_dtype=F32)[0]
+    flush = torch.empty(1 << 29, dtype=torch.uint8, device="cuda:0")  # larger than every cache
+    for i in range(6):
+        if i % 2:
+            flush.fill_(i)
+        assert torch.equal(f(*ops, None, m, n, k, act=act, out_dtype=F32)[0], want), i
