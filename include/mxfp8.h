@@ -484,7 +484,8 @@ mx_status mx_grouped_mm_bf16_fwd_epilogue(const uint16_t* a, const uint16_t* b, 
  *   dy     [m x n_out] bf16 (n_out = n, or n/2 for MX_ACT_SWIGLU), the gradient of out
  *   pre    [m x n] bf16, the forward's z (not read for MX_ACT_NONE, may then be NULL)
  *   dpre   [m x n] bf16 (written) = dy * act'(z): the grad_out of the product (its casts
- *          feed mx_grouped_mm_dgrad and mx_grouped_mm_wgrad). Rows of no group are 0.
+ *          feed mx_grouped_mm_dgrad and mx_grouped_mm_wgrad). Rows of no group are 0. For
+ *          MX_ACT_RELU dy where z > 0, else 0, whatever dy is there.
  *          May be NULL for MX_ACT_NONE, where it is dy (a call for dbias alone)
  *   dbias  [groups x n] float32 (written; NULL: not wanted) = sum of group g's rows of
  *          dpre before its rounding, added in an order that depends on offs alone; an

@@ -7,9 +7,8 @@
 
 namespace mx {
 
-// act'(z) for the pointwise activations (sigmoidf as in the forward).
+// act'(z) for the smooth pointwise activations (sigmoidf as in the forward).
 __device__ inline float act_slope(float z, int act) {
-  if (act == ACT_RELU) return z > 0.f ? 1.f : 0.f;
   if (act == ACT_GELU) {
     const float s = sigmoidf(kGelu0 * z * (1.f + kGelu1 * z * z));
     return s + z * s * (1.f - s) * kGelu0 * (1.f + 3.f * kGelu1 * z * z);
@@ -19,6 +18,13 @@ __device__ inline float act_slope(float z, int act) {
     return s * (1.f + z * (1.f - s));
   }
   return 1.f;
+}
+
+// dy act'(z). ReLU's is a choice, not a product: what z <= 0 cuts off is 0 also for an infinite or
+// NaN dy.
+__device__ inline float act_grad(float dy, float z, int act) {
+  if (act == ACT_RELU) return z > 0.f ? dy : 0.f;
+  return dy * act_slope(z, act);
 }
 
 __device__ inline float bf16_f32(uint16_t b) { return __builtin_bit_cast(float, (unsigned)b << 16); }
@@ -114,7 +120,7 @@ __global__ __launch_bounds__(256) void k_epi_bwd(EpiBwdArgs p) {
             dg[i] = dy[i] * u[i] * s * (1.f + z[i] * (1.f - s));
             du[i] = dy[i] * z[i] * s;
           } else {
-            dg[i] = dy[i] * act_slope(z[i], p.act);
+            dg[i] = act_grad(dy[i], z[i], p.act);
           }
           sg[i] += dg[i];
           if (GLU) su[i] += du[i];

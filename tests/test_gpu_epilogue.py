@@ -435,3 +435,20 @@ def test_forward_long_contractions_same_bits(kind, m, n, k, act):
         if i % 2:
             flush.fill_(i)
         assert torch.equal(f(*ops, None, m, n, k, act=act, out_dtype=F32)[0], want), i
+
+
+def test_backward_relu_keeps_what_is_cut_off_out():
+    """ReLU's gradient is a choice, dy or 0: an infinite or NaN dy where z <= 0 reaches neither
+    dpre nor dbias, and where z > 0 it passes."""
+    m, n = 70, 72
+    z = torch.randn(m, n, device="cuda:0").bfloat16()
+    dy = torch.randn(m, n, device="cuda:0").bfloat16()
+    z[:, :4] = -z[:, :4].abs() - 0.5
+    z[3, 2], z[4, 3] = 0.0, -0.0
+    dy[1, 0], dy[2, 1], dy[3, 2], dy[4, 3] = float("inf"), float("nan"), float("-inf"), float("nan")
+    z[5, 8], dy[5, 8] = 1.5, float("inf")
+    got, dbias = mx.mx_epilogue_backward(dy, z, dev_i32([40, 70]), RELU)
+    assert torch.equal(got, torch.where(z > 0, dy, torch.zeros_like(dy)))
+    assert torch.all(dbias[:, :4] == 0)
+    assert dbias[0, 8] == float("inf") and torch.isfinite(dbias[1]).all()
+    assert torch.isfinite(dbias[:, 9:]).all()
