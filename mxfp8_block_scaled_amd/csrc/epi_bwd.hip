@@ -7,15 +7,18 @@
 
 namespace mx {
 
-// act'(z) for the smooth pointwise activations (sigmoidf as in the forward).
+// act'(z) for the smooth pointwise activations (sigmoidf as in the forward). Beyond |z| = 1e4 the
+// sigmoid is 0 or 1 to the last bit and the terms with s (1 - s) vanish: z is clamped in them, whose
+// powers of z would overflow and leave 0 * inf.
 __device__ inline float act_slope(float z, int act) {
+  const float zc = fminf(fmaxf(z, -1e4f), 1e4f);
   if (act == ACT_GELU) {
     const float s = sigmoidf(kGelu0 * z * (1.f + kGelu1 * z * z));
-    return s + z * s * (1.f - s) * kGelu0 * (1.f + 3.f * kGelu1 * z * z);
+    return s + zc * s * (1.f - s) * kGelu0 * (1.f + 3.f * kGelu1 * zc * zc);
   }
   if (act == ACT_SILU) {
     const float s = sigmoidf(z);
-    return s * (1.f + z * (1.f - s));
+    return s * (1.f + zc * (1.f - s));
   }
   return 1.f;
 }
@@ -116,9 +119,9 @@ __global__ __launch_bounds__(256) void k_epi_bwd(EpiBwdArgs p) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           if (GLU) {
-            const float s = sigmoidf(z[i]);
-            dg[i] = dy[i] * u[i] * s * (1.f + z[i] * (1.f - s));
-            du[i] = dy[i] * z[i] * s;
+            // the factor that may be small first: dy u and dy z alone can overflow
+            dg[i] = dy[i] * act_slope(z[i], ACT_SILU) * u[i];
+            du[i] = dy[i] * (z[i] * sigmoidf(z[i]));
           } else {
             dg[i] = act_grad(dy[i], z[i], p.act);
           }

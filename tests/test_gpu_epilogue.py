@@ -452,3 +452,31 @@ def test_backward_relu_keeps_what_is_cut_off_out():
     assert torch.all(dbias[:, :4] == 0)
     assert dbias[0, 8] == float("inf") and torch.isfinite(dbias[1]).all()
     assert torch.isfinite(dbias[:, 9:]).all()
+
+
+@pytest.mark.parametrize("act", [GELU, SILU, SWIGLU])
+def test_backward_of_large_values(oracle, act):
+    """Finite z, dy and gradients far beyond where the activations saturate: slopes 0 and 1."""
+    far = np.array([-3e38, -1e30, -2e19, -1e10, -3e4, -200, 200, 3e4, 1e10, 2e19, 1e30, 3e38, 0.0, 1.0, -1.0, 4.0])
+    rows = np.array([1.0, -2.5, 1e-20, 1e30])
+    z_t = torch.from_numpy(np.tile(far, (4, 1)).astype(np.float32)).bfloat16()
+    dy_t = torch.from_numpy(np.tile(rows[:, None], (1, 16)).astype(np.float32)).bfloat16()
+    if act == SWIGLU:  # up values that overflow with dy before the gate's slope makes them small
+        up = np.where(far < -100, 1e25, 0.5)
+        z_t = torch.cat([z_t, torch.from_numpy(np.tile(up, (4, 1)).astype(np.float32)).bfloat16()], 1)
+    z, dy = z_t.double().numpy(), dy_t.double().numpy()
+    with np.errstate(over="ignore"):
+        ref = backward64(dy, z, act)
+    got, dbias = mx.mx_epilogue_backward(dy_t.to("cuda:0"), z_t.to("cuda:0"), None, act)
+    g = val(oracle, got)
+    big = np.abs(ref) > 3.38e38  # beyond bf16: an infinity of the right sign
+    assert np.all(np.isinf(g[big]) & (np.sign(g[big]) == np.sign(ref[big])))
+    ok = ~big
+    # slopes of these z are 0, 1 or moderate: fp32 errors of a few 1e-6, then the rounding; a sigmoid
+    # below fp32's smallest normal number, 2^-126, counts as 0 (e^-200 beside dy u = 1e55)
+    weight = np.abs(np.concatenate([dy, dy], 1) if act == SWIGLU else dy) * (1 + np.abs(z))
+    if act == SWIGLU:
+        weight[:, :16] *= np.abs(z[:, 16:])
+    assert np.all(np.abs(g[ok] - ref[ok]) <=
+                  1.001 * half_ulp_bf16(ref[ok]) + 1e-5 * np.abs(ref[ok]) + 2.0**-126 * weight[ok])
+    assert torch.isfinite(dbias[0]).cpu().numpy()[~big.any(0)].all()
