@@ -567,9 +567,11 @@ int64_t mx_moe_layer_workspace_bytes(int64_t tokens, int64_t hidden, int64_t ffn
  *              the call's work has finished
  * |u|^2 is summed in float64, X is kept in fp32 between the steps and the products take
  * fp16 operands: out is within about 1e-3 (relative, before its bf16 rounding) of the
- * iteration in 64 bits. A zero matrix gives zeros; a matrix with an infinity or NaN gives
- * NaN throughout and leaves the others of the batch alone. Singular values that the
- * coefficients drive beyond about 4 leave fp16's range. The order of every sum is fixed. */
+ * iteration in 64 bits. A zero matrix gives zeros, with eps = 0 too; any finite norm, above
+ * float32's range too, is a norm like others; a u with an infinity (a sum beyond float32's
+ * range is one) or NaN gives NaN throughout and leaves the others of the batch alone.
+ * Singular values that the coefficients drive beyond about 4 leave fp16's range. The order
+ * of every sum is fixed. */
 #define MX_ORTHO_MAX_DIM 65536
 #define MX_ORTHO_MAX_STEPS 64
 mx_status mx_orthogonalize(const void* g, int g_dtype, const float* momentum, float* momentum_out, float mu,

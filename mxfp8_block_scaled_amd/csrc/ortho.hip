@@ -514,12 +514,16 @@ __global__ __launch_bounds__(256) void k_ortho_init(OrthoInput p) {
   for (int i = 0; i < kNormBlocks; i += 64) s += p.norm[b * kNormBlocks + i + l];
 #pragma unroll
   for (int d = 32; d; d >>= 1) s += __shfl_xor(s, d);
-  const float norm = (float)sqrt(s), inv = 1.f / (norm + p.eps);
+  // A norm near or beyond float32's limits is brought back by a power of two, which v below takes
+  // too; a zero matrix with eps = 0 stays zero.
+  const double size = sqrt(s) + (double)p.eps;
+  const float pre = size > 0x1p100 ? 0x1p-100f : size < 0x1p-100 ? 0x1p100f : 1.f;
+  const float norm = (float)(sqrt(s) * pre), div = norm + p.eps * pre, inv = div == 0.f ? 0.f : 1.f / div;
   if (tid == 0 && blockIdx.x == 0 && blockIdx.y == 0) p.part0[b] = norm * inv * norm * inv;
 #pragma unroll
   for (int k = 0; k < 16; ++k) {
     const float v = !p.mom ? u[k] : p.nesterov ? u[k] + p.mu * m[k] : m[k];
-    tile[k * 4 + (tid >> 6)][l] = r0 + k * 4 + (tid >> 6) < p.rows && c0 + l < p.cols ? v * inv : 0.f;
+    tile[k * 4 + (tid >> 6)][l] = r0 + k * 4 + (tid >> 6) < p.rows && c0 + l < p.cols ? v * pre * inv : 0.f;
   }
   __syncthreads();
   const int64_t pb = b * p.rows_p * p.cols_p;

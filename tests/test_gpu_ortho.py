@@ -208,3 +208,23 @@ def test_refusals():
     assert mx.mx_orthogonalize_workspace_bytes(1, 65536, 8) > 0
     with pytest.raises(ValueError):
         mx.mx_orthogonalize_workspace_bytes(1, 65537, 8)
+
+
+def test_norms_at_the_limits_of_float32():
+    """eps = 0: a zero matrix gives zeros; norms below and above float32's range are norms like others."""
+    rng = np.random.default_rng(9)
+    base = torch.from_numpy(rng.standard_normal((72, 40)).astype(np.float32))
+    g = torch.stack([torch.zeros(72, 40), base * 1e-41, base.clamp(-2, 2) * 1.7e38, base, base * 1e-36])
+    assert torch.isfinite(g).all() and g[2].double().norm() > 3.4e38
+    for eps in (0.0, 1e-42):
+        out = val(mx.mx_orthogonalize(g.to("cuda:0"), eps=eps)[0])
+        assert np.all(out[0] == 0)
+        for i in range(1, 5):
+            check(out[i], newton_schulz(g[i].double().numpy(), eps=eps), f"eps {eps} [{i}]")
+    assert np.all(val(mx.mx_orthogonalize(torch.zeros(300, 200, device="cuda:0"), eps=0.0)[0]) == 0)
+    # with momentum: the update's norm counts, not the gradient's
+    m = torch.from_numpy(rng.standard_normal((5, 72, 40)).astype(np.float32))
+    m[0] = 0
+    out, new = mx.mx_orthogonalize(torch.zeros_like(g).to("cuda:0"), momentum=m.to("cuda:0"), mu=0.5, eps=0.0)
+    assert np.all(val(out)[0] == 0) and torch.equal(new.cpu(), 0.5 * m)
+    check(val(out)[1], newton_schulz(0.25 * m[1].double().numpy(), eps=0.0), "momentum alone")
