@@ -509,8 +509,11 @@ int64_t mx_epilogue_backward_workspace_bytes(int32_t groups, int grouped, int64_
  *            lowest index; a NaN logit counts as -infinity
  *   weight   MX_SCORE_SOFTMAX: softmax over all experts; MX_SCORE_SIGMOID: 1 / (1 +
  *            exp(-logit)); renormalize != 0 divides by the sum over the chosen ones;
- *            all are multiplied by `scale`. A score below float32's normal range is 0. An expert masked with a logit of -infinity
- *            has weight 0 and is not computed, also when too few others are left
+ *            all are multiplied by `scale` (positive, finite). A score below float32's
+ *            normal range is 0; a logit of +infinity counts as the largest finite float
+ *            (several share the weight, with one of that value too). An expert masked with a
+ *            logit of -infinity has weight 0 and is not computed, also when too few others
+ *            are left
  *   layer    z = W1_e x_t, h = silu(z[0, ffn)) * z[ffn, 2 ffn),
  *            out_t = sum_j weight_tj W2_e h (+ residual_t), e = the j-th choice
  * Experts [expert_first, expert_first + experts_local) of the `experts` routed ones are
@@ -528,9 +531,11 @@ int64_t mx_epilogue_backward_workspace_bytes(int32_t groups, int grouped, int64_
  *   workspace mx_moe_layer_workspace_bytes(tokens, hidden, ffn, topk) bytes, in use until the
  *             call's work has finished
  * 0 <= tokens <= MX_MOE_MAX_TOKENS; hidden and ffn multiples of 32, one expert's w1
- * below 2^31 bytes; tokens * ld_x < 2^30, tokens * topk * ffn < 2^29; logits 4-byte aligned. Activations stay bf16 (x) and twice bf16 (h): nothing is quantized but the
- * weights, and all sums are fp32. Results do not depend on timing: no sum is formed by
- * atomics. mx_moe_layer_bf16 takes the weights as bf16 without scales. */
+ * below 2^31 bytes; tokens * ld_x < 2^30, tokens * topk * ffn < 2^29; logits 4-byte aligned.
+ * Activations stay bf16 (x) and twice bf16 (h): nothing is quantized but the weights, and
+ * all sums are fp32. Results do not depend on timing: the order of every sum is fixed by
+ * the routing, and none is formed by atomics. mx_moe_layer_bf16 takes the weights as bf16
+ * without scales. */
 #define MX_MOE_MAX_TOKENS 256
 #define MX_MOE_MAX_EXPERTS 1024
 #define MX_MOE_MAX_TOPK 32

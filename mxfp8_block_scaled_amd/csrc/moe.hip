@@ -634,8 +634,8 @@ __global__ __launch_bounds__(64 * kWaves, few_waves(W)) void k_moe_up_many(MoeAr
 // One block per 128 output columns and split of the work: the chosen experts' contractions,
 // run after run (an expert with more than RUN tokens takes several runs), are cut evenly into
 // p.splits pieces; each writes its sums as one partial, [splits][tokens][hidden]. A wave's
-// sums of up to 64 tokens stay in LDS; more are added up in the partial itself, by atomics
-// that never meet: a value belongs to one wave, which adds to it in the order of its runs.
+// sums of up to 64 tokens stay in LDS; more are added up in the partial itself: a value belongs
+// to one wave, which reads, adds and writes it in the order of its runs.
 template <int W, bool IN_LDS>
 __global__ __launch_bounds__(64 * kWaves, few_waves(W)) void k_moe_down_many(MoeArgs p) {
   constexpr int HT = down_tiles(IN_LDS), RUN = 16 * HT;
@@ -700,7 +700,7 @@ __global__ __launch_bounds__(64 * kWaves, few_waves(W)) void k_moe_down_many(Moe
   Rows<W> rows = expert_rows<W>(p.w2, p.w2_s, 0, p.hidden, p.ffn, (int)row0);
   // this thread's part of the tile: high or low part, token (tid / 16) % 16 of each 16, chunk tid % 16
   const int part_of = tid >> 8, tok = (tid >> 4) & 15;
-  const uint16_t* hs[HT];
+  unsigned hs[HT];  // element offset of a slot's part, ~0: none
   auto start = [&]() {
     which = (which + 1) & 3;
     int* list = lists[which][wave];
@@ -718,13 +718,13 @@ __global__ __launch_bounds__(64 * kWaves, few_waves(W)) void k_moe_down_many(Moe
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
     for (int i = 0; i < HT; ++i)
-      hs[i] = 16 * i + tok < n ? p.h + ((int64_t)list[16 * i + tok] * 2 + part_of) * p.ffn + (tid & 15) * 8 : nullptr;
+      hs[i] = 16 * i + tok < n ? ((unsigned)list[16 * i + tok] * 2 + part_of) * (unsigned)p.ffn + (tid & 15) * 8 : ~0u;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   };
   auto load = [&](Flight& o, int at) {
     const bool in = s * 128 + (tid & 15) * 8 < p.ffn;
 #pragma unroll
-    for (int i = 0; i < HT; ++i) o.h[i] = hs[i] && in ? *(const u32x4*)(hs[i] + s * 128) : (u32x4){0, 0, 0, 0};
+    for (int i = 0; i < HT; ++i) o.h[i] = hs[i] != ~0u && in ? *(const u32x4*)(p.h + s * 128 + hs[i]) : (u32x4){0, 0, 0, 0};
     o.w = load_block<W>(rows, s);
     o.n = n;
     o.list = which;
@@ -764,18 +764,31 @@ __global__ __launch_bounds__(64 * kWaves, few_waves(W)) void k_moe_down_many(Moe
           for (int half = 0; half < 2; ++half)
             acc[i] = mfma16(w[q], __builtin_bit_cast(bf16x8, stage[buf][half][staged(16 * i + (l & 15), 4 * g + q)]), acc[i]);
       }
-      if (cur.last) {  // the run's sums, into its tokens' sums
+      if (cur.last) {
+        // The run's sums, into its tokens' sums (a run holds a token once). Places past the run
+        // or past the columns read what the last ones do and write nothing: a branch around
+        // each load would wait for each.
+        const int64_t col = wrow + g * 4 < p.hidden ? wrow + g * 4 : p.hidden - 4;
+        float share[HT];
+        unsigned t[HT];
 #pragma unroll
         for (int i = 0; i < HT; ++i) {
-          if (16 * i + (l & 15) < cur.n) {
-            const int slot = lists[cur.list][wave][16 * i + (l & 15)], t = slot / p.topk;
-            const v4f y = p.weights[slot] * acc[i];
-            if constexpr (IN_LDS) {
-              *(v4f*)&tot[wave][t][g * 4] += y;
-            } else if (wrow + g * 4 < p.hidden) {
+          const int at = 16 * i + (l & 15), slot = lists[cur.list][wave][at < cur.n ? at : cur.n - 1];
+          share[i] = p.weights[slot];
+          t[i] = slot / p.topk;
+        }
+        v4f sum[HT];
 #pragma unroll
-              for (int r = 0; r < 4; ++r) unsafeAtomicAdd(part + (int64_t)t * p.hidden + wrow + g * 4 + r, y[r]);
-            }
+        for (int i = 0; i < HT; ++i) {
+          if constexpr (IN_LDS) sum[i] = *(const v4f*)&tot[wave][t[i]][g * 4];
+          else sum[i] = *(const v4f*)(part + col + t[i] * p.hidden);
+        }
+#pragma unroll
+        for (int i = 0; i < HT; ++i) {
+          sum[i] += share[i] * acc[i];
+          if (16 * i + (l & 15) < cur.n) {
+            if constexpr (IN_LDS) *(v4f*)&tot[wave][t[i]][g * 4] = sum[i];
+            else if (wrow + g * 4 < p.hidden) *(v4f*)(part + col + t[i] * p.hidden) = sum[i];
           }
           acc[i] = (v4f){0.f, 0.f, 0.f, 0.f};
         }

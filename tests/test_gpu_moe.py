@@ -258,3 +258,24 @@ def test_refusals(oracle):
         lay.call(x, lg, 2, residual=dev_bf16(lay.res)[:1])
     with pytest.raises(ValueError):
         mx.mx_moe_layer_workspace_bytes(257, 32, 32, 2)
+
+
+@pytest.mark.parametrize("kind", ["mx", "bf16"])
+@pytest.mark.parametrize("tokens", [65, 130, 256])
+def test_many_tokens_same_bits(oracle, kind, tokens):
+    """Above 64 tokens an expert's tokens take several runs, whose sums meet in memory: the same
+    bits on every call, and the definition's values."""
+    H, F, E, topk = 288, 160, 7, 5
+    lay = Layer(oracle, tokens, tokens, H, F, E, kind)
+    logits = lay.rng.standard_normal((tokens, E)).astype(np.float32)
+    x, lg, res = dev_bf16(lay.x), torch.from_numpy(logits).to("cuda:0"), dev_bf16(lay.res)
+    want = lay.call(x, lg, topk, residual=res, out_dtype=mx.MX_OUT_F32)
+    ids, w = choose(logits, topk, mx.MX_SCORE_SOFTMAX, True, 1.0)
+    assert np.array_equal(host(want[1]), ids)
+    close(host(want[0]).astype(np.float64), lay.ref(ids, w, 0, True), F32_TOL, "y")
+    flush = torch.empty(1 << 29, dtype=torch.uint8, device="cuda:0")
+    for i in range(6):
+        if i % 2:
+            flush.fill_(i)
+        again = lay.call(x, lg, topk, residual=res, out_dtype=mx.MX_OUT_F32)
+        assert all(torch.equal(a, b) for a, b in zip(again, want)), i

@@ -114,3 +114,16 @@ def test_orthogonalize(lib):
     assert call(coefs=(1.0, 17.0, 0.0) * 2) == MX_E_SHAPE and call(coefs=(float("nan"), 0.0, 0.0) * 2) == MX_E_SHAPE
     assert call(nb=need(2, 40, 24)) == MX_E_DEVICE and call(nb=need(2, 40, 24) - 1) == MX_E_SHAPE
     assert call(ws=None) == MX_E_SHAPE and need(1, 0, 8) == -1 and need(65536, 8, 8) == -1
+
+
+def test_moe_layer_forms_no_sum_by_atomics():
+    """The header's promise: the layer's kernels have no atomic operation on floats (the integer
+    ones build lists and bitmaps in LDS)."""
+    import os
+    import re
+
+    path = os.path.join(os.path.dirname(_lib.LIB_PATH), "csrc", "moe.hip")
+    with open(path) as f:
+        code = re.sub(r"//[^\n]*", "", f.read())
+    assert "unsafeAtomicAdd" not in code and "atomic_fadd" not in code
+    assert set(re.findall(r"atomic\w*\((&?\w+)", code)) <= {"&bits", "&n_list", "&cnt"}
