@@ -480,3 +480,41 @@ def test_backward_of_large_values(oracle, act):
     assert np.all(np.abs(g[ok] - ref[ok]) <=
                   1.001 * half_ulp_bf16(ref[ok]) + 1e-5 * np.abs(ref[ok]) + 2.0**-126 * weight[ok])
     assert torch.isfinite(dbias[0]).cpu().numpy()[~big.any(0)].all()
+
+
+# ---- large products and gradients ----------------------------------------------------------
+LARGE = [
+    # two rounds of 256x256 tiles and a short one, whose tiles run as quarters
+    ("mx", 8448, 4096, 1056, [4128, 0, 4320], SWIGLU, True, True, True, BF16),
+    ("mx", 8448, 4096, 1056, [4128, 0, 4320], SILU, True, True, False, BF16),
+    ("bf16", 8448, 4104, 1032, [1, 4200, 4247], GELU, True, True, True, BF16),
+]
+
+
+@pytest.mark.parametrize("case", LARGE, ids=["-".join(map(str, c[:4])) + f"-act{c[5]}" for c in LARGE])
+def test_forward_short_last_round(oracle, case):
+    test_forward(oracle, case)
+
+
+@pytest.mark.parametrize("m,n,sizes,act", [(16384, 1040, [4096, 0, 33, 8000, 4000], SWIGLU),
+                                           (16384, 1032, None, GELU), (4001, 1041, [1, 4000], SILU),
+                                           (6000, 2002, None, SWIGLU)])
+def test_backward_64_row_tiles(oracle, m, n, sizes, act):
+    test_backward(oracle, m, n, sizes, act, True)
+
+
+@pytest.mark.parametrize("kind,m,n,k,act", [("mx", 96, 128, 1056, SWIGLU), ("mx", 40, 72, 4128, SILU),
+                                            ("bf16", 1024, 2304, 128, GELU), ("mx", 4096, 4160, 1056, SWIGLU)])
+def test_a_row_of_nan_stays_alone(oracle, kind, m, n, k, act):
+    """NaN in one row of A reaches that row of out and z alone, also across a tile's rows."""
+    a = torch.randn(m, k, device="cuda:0").bfloat16()
+    b = (torch.randn(n, k, device="cuda:0") * k**-0.5).bfloat16()
+    ops = [a, b] if kind == "bf16" else [*mx.mx_quantize_dim0(a), *mx.mx_quantize_dim0(b)]
+    f = mx.mx_grouped_mm_bf16_fwd_epilogue if kind == "bf16" else mx.mx_grouped_mm_fwd_epilogue
+    want, z = f(*ops, None, m, n, k, act=act, save_pre=True)
+    bad = ops[0].clone()
+    bad.view(m, k)[m // 2] = float("nan") if kind == "bf16" else 0x7F  # 0x7F: the NaN code
+    got, z2 = f(bad, *ops[1:], None, m, n, k, act=act, save_pre=True)
+    rest = torch.arange(m, device="cuda:0") != m // 2
+    assert torch.equal(got[rest], want[rest]) and torch.equal(z2[rest], z[rest])
+    assert torch.isnan(got[m // 2]).all() and torch.isnan(z2[m // 2]).all()

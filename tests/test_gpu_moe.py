@@ -279,3 +279,38 @@ def test_many_tokens_same_bits(oracle, kind, tokens):
             flush.fill_(i)
         again = lay.call(x, lg, topk, residual=res, out_dtype=mx.MX_OUT_F32)
         assert all(torch.equal(a, b) for a, b in zip(again, want)), i
+
+
+# Contractions that go round the prefetch of every kernel: 33 and 32 steps of 128 elements over
+# eight waves in the gate/up products, and a down product whose steps cross experts in every wave
+# (5 experts of 9 steps, the last one short). Per batch size the kernels with 4, 8 and 16 columns,
+# the ones for more tokens in one pass and in several.
+LONG = [(t, 4128, 96, 3, 0, 3, 3, 0, True, 1.0) for t in (1, 4, 6, 8, 12, 40, 64, 130)]
+LONG += [(12, 4128, 352, 3, 0, 3, 2, 0, True, 1.0), (3, 4096, 64, 4, 1, 2, 4, 1, True, 1.0),
+         (70, 4096, 64, 4, 1, 2, 4, 1, True, 1.0)]
+LONG += [(t, 96, 1120, 5, 0, 5, 5, 1, True, 1.0) for t in (1, 4, 6, 12, 40, 64, 130, 256)]
+LONG += [(t, 160, 2080, 6, 0, 6, 3, 0, True, 1.0) for t in (2, 7, 15, 33, 100)]
+
+
+@pytest.mark.parametrize("kind", ["mx", "bf16"])
+@pytest.mark.parametrize("case", LONG, ids=["-".join(str(v) for v in c[:7]) for c in LONG])
+def test_long_contractions(oracle, case, kind):
+    test_matches_definition(oracle, (*case, kind), mx.MX_OUT_F32, True)
+
+
+@pytest.mark.parametrize("kind", ["mx", "bf16"])
+@pytest.mark.parametrize("tokens", [3, 8, 14, 40, 100])
+def test_a_token_of_nan_stays_alone(oracle, kind, tokens):
+    """NaN and infinity in one token's x reach that token's output alone, whichever tokens share its expert."""
+    H, F, E, topk = 416, 288, 4, 2
+    lay = Layer(oracle, tokens, tokens, H, F, E, kind)
+    logits = torch.from_numpy(lay.rng.standard_normal((tokens, E)).astype(np.float32)).to("cuda:0")
+    x = dev_bf16(lay.x)
+    want = lay.call(x, logits, topk, out_dtype=mx.MX_OUT_F32)[0]
+    bad = x.clone()
+    bad[1] = float("nan")
+    bad[tokens - 1, 5] = float("inf")
+    got = lay.call(bad, logits, topk, out_dtype=mx.MX_OUT_F32)[0]
+    rest = [t for t in range(tokens) if t not in (1, tokens - 1)]
+    assert torch.equal(got[rest], want[rest])
+    assert torch.isnan(got[1]).all()

@@ -228,3 +228,32 @@ def test_norms_at_the_limits_of_float32():
     out, new = mx.mx_orthogonalize(torch.zeros_like(g).to("cuda:0"), momentum=m.to("cuda:0"), mu=0.5, eps=0.0)
     assert np.all(val(out)[0] == 0) and torch.equal(new.cpu(), 0.5 * m)
     check(val(out)[1], newton_schulz(0.25 * m[1].double().numpy(), eps=0.0), "momentum alone")
+
+
+# 128x128 tiles in the step product (the sizes between one round of 64x64 tiles and 192 of
+# 256x256): a batch, a ragged one, a tall one
+MIDDLE = [
+    (8, 512, 512, "gauss", torch.float32),
+    (1, 2048, 2040, "lowrank", torch.bfloat16),
+    (3, 700, 1410, "decay", torch.float32),
+    (2, 1801, 640, "gauss", torch.bfloat16),
+]
+
+
+@pytest.mark.parametrize("case", MIDDLE, ids=["-".join(map(str, c[:4])) for c in MIDDLE])
+def test_128_tiles(case):
+    test_matches_float64(case)
+
+
+def test_a_matrix_of_nan_stays_alone_in_128_tiles():
+    g = torch.randn(8, 520, 500, device="cuda:0")
+    want = mx.mx_orthogonalize(g)[0]
+    bad = g.clone()
+    bad[3, 100, 100] = float("nan")
+    bad[5, 0, 499] = float("inf")
+    got = mx.mx_orthogonalize(bad)[0]
+    rest = [0, 1, 2, 4, 6, 7]
+    assert torch.equal(got[rest], want[rest])
+    assert torch.isnan(got[3]).all() and torch.isnan(got[5]).all()
+    again = mx.mx_orthogonalize(g)[0]
+    assert torch.equal(again, want)
