@@ -345,15 +345,15 @@ __device__ inline int64_t udiv(int64_t a, int64_t b) {
 }
 __device__ inline int64_t umod(int64_t a, int64_t b) { return a - udiv(a, b) * b; }
 
+// Tiles on and above the diagonal of a square grid of nt x nt, in bands of four rows: in a
+// band, column by column from the diagonal on (1, 2, 3, then 4 rows each).
+__host__ __device__ inline int64_t triangle_tiles(int64_t nt) { return nt * (nt + 1) / 2; }
+
 // Logical tile t -> its output tile and contraction range (one block per tile).
 // Each XCD takes a contiguous range of logical tiles in order (xcd_remap,
 // spread_tiles); with a raster, over `mt_count` m-tiles, of bands of GM m-tiles by all n-tiles,
 // the ~32 tiles in flight on one XCD share their A and B slices in its L2 (GM = 4
 // measured best among 1..16).
-// Tiles on and above the diagonal of a square grid of nt x nt, in bands of four rows: in a
-// band, column by column from the diagonal on (1, 2, 3, then 4 rows each).
-__host__ __device__ inline int64_t triangle_tiles(int64_t nt) { return nt * (nt + 1) / 2; }
-
 template <int BM, int BN, int MODE, int OUT_BF16, int EL, int EP = EP_NONE>
 __device__ inline Tile tile_at(const GemmArgs& p, int64_t t, int64_t mt_count, const GroupChunk& first) {
   constexpr int64_t GM = 4;

@@ -14,12 +14,15 @@
 // Routing is a wave per token (topk rounds of a wave maximum): inside k_moe_up for up to 8
 // tokens, else k_moe_route. Every sum has an order that depends on the routing alone.
 //
-// Bound by HBM. 32 experts, hidden 7168, ffn 2048, top 8: one token 75 us (k_moe_up 48, k_moe_down
-// 29) for 363 MB, 4.8 TB/s; 64 tokens 294 us (183 + 115 + 5 + 5) for 1.45 GB, 4.9 TB/s, where a 1
-// GiB device copy moves 5.05 TB/s.
+// Bound by HBM up to 64 tokens. 32 experts, hidden 7168, ffn 2048, top 8: one token 75 us (k_moe_up
+// 48, k_moe_down 29) for 363 MB, 4.8 TB/s; 64 tokens 294 us (183 + 115 + 5 + 5) for 1.45 GB, 4.9
+// TB/s, where a 1 GiB device copy moves 5.05 TB/s; bf16 weights 150 us for 705 MB and 660 us for
+// 2.8 GB. Above, by the latency of each step's loads (see k_moe_up_many): 200 tokens 496 us, 2.9
+// TB/s, and 811 with bf16 weights; 109 tokens of 128 experts of 704 x 384 61 us, 1.7 TB/s.
 // The products run on v_mfma_f32_16x16x32_bf16 with weight rows as the first operand and
 // tokens as the second (up to 16 tokens per instruction): codes become bf16 in registers,
-// exactly (E4M3 times a power of two), x is bf16 as given, and h goes to the second product
+// exactly (E4M3 times a power of two; scale bytes 0 to 2 reach below bf16's smallest number, and
+// codes lose bits there), x is bf16 as given, and h goes to the second product
 // as the sum of two bf16 values (16 bits of significand), since one alone would cost as much
 // accuracy as the rounding of the result.
 
@@ -239,10 +242,6 @@ __device__ inline void to_bf16(const RawBlock<W>& r, bf16x8 o[4]) {
   }
 }
 
-__device__ inline bf16x8 load8(const uint16_t* src, bool in) {
-  return __builtin_bit_cast(bf16x8, in ? *(const u32x4*)src : (u32x4){0, 0, 0, 0});
-}
-
 __device__ inline v4f mfma16(bf16x8 a, bf16x8 b, v4f c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
@@ -285,14 +284,17 @@ __device__ inline void store_y(const MoeArgs& p, int64_t o, float y) {
 __device__ inline int staged(int r, int c) { return r * 16 + (c ^ (r & 15)); }
 
 // ---- up to 16 tokens: the waves of a block share weight rows and split the contraction ----
-// A wave keeps DEPTH steps in registers, so that the weights in flight (16 waves of 2 KB a
-// row tile and step on a compute unit) cover HBM's latency. The tokens' values of a step are
-// loaded as whole 256-byte rows, TQ 16-byte pieces a lane (4 rows each), and turned to the
+// A wave issues the loads of a step DEPTH - 1 steps ahead, so that the weights in flight (16 waves
+// of 2 KB a row tile and step on a compute unit) cover HBM's latency. The sets of registers are
+// handed on by copies, which wait for the loads into them: as compiled a wave waits for all of
+// its loads once a step, and it is the number of waves that keeps HBM busy. The tokens' values
+// of a step are loaded as whole 256-byte rows, TQ 16-byte pieces a lane (4 rows each), and turned to the
 // matrix operand's layout through a piece of LDS of the wave's own. Columns past the expert's
 // tokens hold anything: a column of the product depends on its own token alone.
 
-// Steps in flight: MXFP8 at 128 registers and two blocks on a compute unit; bf16 steps are
-// twice as large and take 256 registers and one block.
+// Sets of registers: MXFP8 at 128 registers and two blocks on a compute unit; bf16 steps are
+// twice as large and take 256 registers and one block. (k_moe_down at 16 columns spills, 10
+// registers with MXFP8 weights and 3 with bf16.)
 constexpr int few_waves(int w) { return w == W_MXFP8 ? 4 : 2; }
 constexpr int up_depth(int w, int tq) { return w == W_BF16 || tq == 1 ? 3 : 2; }
 constexpr int down_depth(int w, int tq) { return w == W_BF16 ? 4 : tq == 1 ? 4 : tq == 2 ? 3 : 2; }
@@ -536,10 +538,12 @@ __global__ __launch_bounds__(64 * kWaves, few_waves(W)) void k_moe_down(MoeArgs 
 // ---- more tokens: the waves of a block share the tokens, in LDS, and split the weight rows ----
 // With 16 tokens to an expert a wave that streams 16 rows of codes needs as many bytes of x,
 // and four times as many of h: read through LDS, each of them comes from L2 once per 128
-// rows. Three steps of weights and tokens are in flight (two on their way, one in use).
+// rows. Loads are issued two steps ahead of their use; handing the sets of registers on by copies
+// waits for them at the end of each step, so a step costs the latency of its loads.
 
 constexpr int kChunk = 64;    // tokens per pass of the kernels below
-// k_moe_down_many: token tiles of one run (an expert with more tokens takes several)
+// k_moe_down_many: token tiles of one run (an expert with more tokens takes several). Four with
+// MXFP8 weights spill 8 registers around the start of a run.
 constexpr int down_tiles(bool in_lds) { return in_lds ? 2 : 4; }
 
 // One block per chosen expert and 64 gate + 64 up rows: waves 0-3 take the gate rows, 4-7 the up rows.

@@ -6,7 +6,8 @@ those epilogues. The same weights serve `mx_moe_layer` for a few tokens at a tim
   y = h W2_e^T + b2_e (+ residual)               for the rows of expert e
 
 x [M, K] bf16 in groups of rows by `offs` (int32 ends, multiples of 32); W1 [E, 2F, K] and
-W2 [E, K, F]. Every step runs in the library's kernels; this module only orders the calls.
+W2 [E, K, F]. Rows past the last end belong to no expert: those of y and dx are left unwritten, and
+they enter no other result. Every step runs in the library's kernels; this module only orders the calls.
 """
 
 from . import (MX_ACT_NONE, MX_ACT_SWIGLU, MX_OUT_F32, mx_epilogue_backward, mx_grouped_mm_dgrad,
