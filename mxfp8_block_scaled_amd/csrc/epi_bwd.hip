@@ -204,7 +204,7 @@ hipError_t launch_bwd(const EpiBwdArgs& p, hipStream_t stream) {
 }
 
 // Rows per tile: 64, or 16 where 64-row tiles would be fewer than two blocks per compute unit (a
-// wave's chain of rows is then what takes the time: 1001 x 576 in 28 us with 64 rows).
+// wave's chain of rows is then what takes the time: 1001 x 576 GELU 33 us with 64 rows, 9 with 16).
 int bwd_rows(int groups, int has_offs, int64_t m, int64_t n_out) {
   const int64_t tiles = (m + 63) / 64 + (has_offs ? groups : 0), v = n_out % 8 == 0 ? 8 : 1;
   return tiles * ((n_out + kBwdCols * v - 1) / (kBwdCols * v)) >= 512 ? 64 : 16;

@@ -237,15 +237,15 @@ namespace {
 // 32x32 where contraction rows above 4 KB then still leave units idle (kernel us, the kernel of
 // gemm.hip / 64x64 / 32x64 / 32x32: 32 x 4096 over 4096 MXFP8 20 / 10 / 8 / 8, bf16 31 / 16 / 16
 // / 11; 512 x 512 over 4096 MXFP8 19 / 10 / 8 / 8, bf16 30 / 20 / 15 / 12; 1024 x 1024 over 4096
-// MXFP8 20 / 14 / 18 / 19; above: 512 x 4096 over 4096 21 / 29 / 35 / 36). Then few output tiles take quarter-size ones, short contractions and little more than
-// half a round of the compute units 128x256 tiles, two blocks per unit, all else 256x256 ones
-// with two waves per SIMD (one wave holding 256 sums is no faster beside a residual, 660 to 667
-// against 655 to 666 for 32768 x 7168 over 2048, and spills without one); two
-// rounds and more of a bf16 output with groups run whole rounds and then the quarters of a
-// short last one. Measured, us at 128x128 / 128x256 / 256x256: 2048 x 2048 x 2048 29 / 48 / 53
-// (bf16, 64 tiles of 256x256); 4096 x 2048 x 4096 46 / 41 / 45 (128 tiles); 4096 x 2560 x 2048
-// 45 / 47 / 41 (160); 4096 x 2816 x 4096 bf16 115 / 125 / 96 (176); 8 groups, 16384 x 4096 x
-// 4096 353 / 302 / 282, and 269 with the quarters.
+// MXFP8 20 / 14 / 18 / 19; above: 512 x 4096 over 4096 21 / 29 / 35 / 36). Then few output tiles
+// take quarter-size ones, short contractions and little more than half a round of the compute
+// units 128x256 tiles, two blocks per unit, all else 256x256 ones with two waves per SIMD (one
+// wave holding 256 sums is no faster beside a residual, 660 to 667 against 655 to 666 for 32768 x
+// 7168 over 2048, and spills without one); two rounds and more of a bf16 output with groups run
+// whole rounds and then the quarters of a short last one. Measured, us at 128x128 / 128x256 /
+// 256x256: 2048 x 2048 x 2048 29 / 48 / 53 (bf16, 64 tiles of 256x256); 4096 x 2048 x 4096 46 /
+// 41 / 45 (128 tiles); 4096 x 2560 x 2048 45 / 47 / 41 (160); 4096 x 2816 x 4096 bf16 115 / 125 /
+// 96 (176); 8 groups, 16384 x 4096 x 4096 353 / 302 / 282, and 269 with the quarters.
 template <int TM, int TN, int EL, int OUT, int EP>
 hipError_t launch_epi_small(mx::EpiArgs p, hipStream_t stream) {
   constexpr int lds = mx::SmallTile<TM, TN, EL>::LDS;
