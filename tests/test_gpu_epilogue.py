@@ -518,3 +518,46 @@ def test_a_row_of_nan_stays_alone(oracle, kind, m, n, k, act):
     rest = torch.arange(m, device="cuda:0") != m // 2
     assert torch.equal(got[rest], want[rest]) and torch.equal(z2[rest], z[rest])
     assert torch.isnan(got[m // 2]).all() and torch.isnan(z2[m // 2]).all()
+
+
+# ---- many groups, no rows, ends out of contract ---------------------------------------------
+MANY = [
+    ("mx", 3264, 64, 64, [32, 0, 32, 64] * 25, SILU, True, True, True, BF16),  # 64x64 tiles
+    ("mx", 9600, 128, 96, [0, 96, 0] * 100, SWIGLU, True, True, True, BF16),  # 128x128 tiles
+    ("bf16", 700, 40, 72, [0, 1, 2, 11] * 50, GELU, True, True, True, F32),
+]
+
+
+@pytest.mark.parametrize("case", MANY, ids=["-".join(map(str, c[:4])) + f"-act{c[5]}" for c in MANY])
+def test_forward_many_groups(oracle, case):
+    test_forward(oracle, case)
+
+
+@pytest.mark.parametrize("act", [NONE, SWIGLU])
+def test_forward_without_rows(act):
+    n, k, G = 128, 96, 3
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda:0")  # noqa: E731
+    w = mx.mx_quantize_dim0(bf(G * n, k))
+    none, s = (torch.zeros(v, dtype=torch.uint8, device="cuda:0") for v in ((0, k), 0))
+    shape = (0, n // 2 if act == SWIGLU else n)
+    for out, z in (mx.mx_grouped_mm_fwd_epilogue(none, s, *w, dev_i32([0] * G), 0, n, k, act=act, save_pre=True),
+                   mx.mx_grouped_mm_bf16_fwd_epilogue(bf(0, k), bf(G * n, k), dev_i32([0] * G), 0, n, k, act=act, save_pre=True),
+                   mx.mx_grouped_mm_bf16_fwd_epilogue(bf(0, k), bf(n, k), None, 0, n, k, act=act, save_pre=True)):
+        assert out.shape == shape and z.shape == (0, n)
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("kind", ["mx", "bf16"])
+@pytest.mark.parametrize("m,n,k", [(192, 64, 1056), (4096, 2304, 96)])
+def test_forward_of_offs_out_of_contract(kind, m, n, k):
+    """Ends that fall or leave [0, m] are read clamped: the rows of a valid reading, no others."""
+    a = torch.randn(m, k, device="cuda:0").bfloat16()
+    b = (torch.randn(3 * n, k, device="cuda:0") * 0.1).bfloat16()
+    ops = (a, b) if kind == "bf16" else (*mx.mx_quantize_dim0(a), *mx.mx_quantize_dim0(b))
+    f = mx.mx_grouped_mm_bf16_fwd_epilogue if kind == "bf16" else mx.mx_grouped_mm_fwd_epilogue
+    got, _ = f(*ops, dev_i32([96, 32, 1 << 30]), m, n, k, act=SILU)
+    want, _ = f(*ops, dev_i32([96, 96, m]), m, n, k, act=SILU)
+    assert torch.equal(got, want)
+    out = torch.full((m, n), 7.0, dtype=torch.bfloat16, device="cuda:0")
+    f(*ops, dev_i32([-5, 96, 64]), m, n, k, act=SILU, out=out)
+    assert torch.all(out[96:] == 7.0) and torch.isfinite(out[:96]).all()
